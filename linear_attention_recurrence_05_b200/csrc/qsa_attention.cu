@@ -356,13 +356,14 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_attention_kernel(const __grid
             }
             // P^T operand: row = column, column = token of this tile (bf16: the second product's
             // operand type; relative error 2^-8 a term at most, independent between terms, so that
-            // the sum's stays below the output's own rounding)
+            // the sum's stays below the output's own rounding).  A column without a score that compares
+            // with its reference (all masked, or NaN) subtracts 0: masked tokens weigh 0, NaN ones NaN.
             unsigned char *pp = sp + (tok >> 6) * (NC * 128) + col0 * 128 + ((tok & 7) << 1);
             const int pc = (tok & 63) >> 3;
 #pragma unroll
             for (int c = 0; c < NCW; ++c) {
                 if (c < 4 * chunks) {
-                    const float x = m[c] == -INFINITY ? 0.f : ex2(s[c] - m[c]);
+                    const float x = ex2(s[c] - (m[c] == -INFINITY ? 0.f : m[c]));
                     l[c] += x;
                     *reinterpret_cast<__nv_bfloat16 *>(pp + c * 128 + ((pc ^ (c & 7)) << 4)) = __float2bfloat16_rn(x);
                 }

@@ -110,10 +110,16 @@ struct Coef {
         }
     }
 };
-// Norm and rotation of one head row held by the D / 8 lanes of a group.  Every lane of the warp
-// takes part.
+// x c + y s with `turn`, else x c (y, which may be infinite or NaN, is another dim's alone)
+__device__ __forceinline__ float turn_dim(float x, float c, float y, float s, bool turn) {
+    float z = x * c;
+    if (turn) z = fmaf(y, s, z);
+    return z;
+}
+// Norm and rotation of one head row held by the D / 8 lanes of a group, of which those with `turn`
+// hold rotated dims.  Every lane of the warp takes part.
 template <int D>
-__device__ __forceinline__ void norm_rope_row(float4 &a, float4 &b, const Coef &k, bool norm, float eps) {
+__device__ __forceinline__ void norm_rope_row(float4 &a, float4 &b, const Coef &k, bool turn, bool norm, float eps) {
     float r = 1.f;
     if (norm) {
         float ss = a.x * a.x, st = b.x * b.x;
@@ -127,10 +133,10 @@ __device__ __forceinline__ void norm_rope_row(float4 &a, float4 &b, const Coef &
         r = rsqrtf(ss * (1.f / D) + eps);
     }
     const float4 x = a, y = b;
-    a = make_float4((x.x * k.ac[0] - y.x * k.bs[0]) * r, (x.y * k.ac[1] - y.y * k.bs[1]) * r,
-                    (x.z * k.ac[2] - y.z * k.bs[2]) * r, (x.w * k.ac[3] - y.w * k.bs[3]) * r);
-    b = make_float4((y.x * k.bc[0] + x.x * k.as[0]) * r, (y.y * k.bc[1] + x.y * k.as[1]) * r,
-                    (y.z * k.bc[2] + x.z * k.as[2]) * r, (y.w * k.bc[3] + x.w * k.as[3]) * r);
+    a = make_float4(turn_dim(x.x, k.ac[0], -y.x, k.bs[0], turn) * r, turn_dim(x.y, k.ac[1], -y.y, k.bs[1], turn) * r,
+                    turn_dim(x.z, k.ac[2], -y.z, k.bs[2], turn) * r, turn_dim(x.w, k.ac[3], -y.w, k.bs[3], turn) * r);
+    b = make_float4(turn_dim(y.x, k.bc[0], x.x, k.as[0], turn) * r, turn_dim(y.y, k.bc[1], x.y, k.as[1], turn) * r,
+                    turn_dim(y.z, k.bc[2], x.z, k.as[2], turn) * r, turn_dim(y.w, k.bc[3], x.w, k.as[3], turn) * r);
 }
 
 // ------------------------------------------------------------------ rows to rows
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(32 * kWarps, 6) qsa_norm_rope_kernel(const __g
             if (h + u * kSub >= h1) break;                // uniform
             const int hh = h + u * kSub + sub;
             float4 a = values(x[u].a), b = values(x[u].b);
-            norm_rope_row<D>(a, b, k, w != nullptr, p.eps);
+            norm_rope_row<D>(a, b, k, 4 * gl < p.half, w != nullptr, p.eps);
             if (hh < h1) {
                 st4(out + hh * D + oa, a);
                 st4(out + hh * D + ob, b);
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(32 * kWarps, 8) qsa_kv_append_kernel(const __g
             if (h + u * kSub >= h1) break;                // uniform
             const int hh = h + u * kSub + sub;
             float4 a = values(x[u].a), c = values(x[u].b);
-            if (is_k) norm_rope_row<D>(a, c, k, p.w_k != nullptr, p.eps);
+            if (is_k) norm_rope_row<D>(a, c, k, 4 * gl < p.half, p.w_k != nullptr, p.eps);
             if (hh < h1) {
                 st4(out + (int64_t)hh * p.page * D + oa, a);
                 st4(out + (int64_t)hh * p.page * D + ob, c);

@@ -448,7 +448,9 @@ static cudaError_t launch_single(AttnParams &p, cudaStream_t s) {
     while (smem_bytes(D, p.ring, entries) > kMaxSmem) --p.ring;
     const uint32_t smem = smem_bytes(D, p.ring, entries);
     auto kern = qsa_attention_kernel<D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the same value at every call: host threads share the attribute, and this call's own size would lower it
+    // between another thread's setting and its launch
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
     if (e != cudaSuccess) return e;
     if (p.split > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;

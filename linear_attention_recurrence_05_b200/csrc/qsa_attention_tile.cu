@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_attention_tile_kernel(const _
     const int tile = p.tiles - 1 - (int)(unit % per_head / (uint32_t)p.B);
     const int n0 = (int)((int64_t)tile * p.Qn / p.tiles), nq = (int)((int64_t)(tile + 1) * p.Qn / p.tiles) - n0;   // <= p.qt
     const int64_t pos0 = (int64_t)p.qpos[b] + n0;
-    // live queries: j0 <= j < j1 (positions >= 0, before the row's count)
-    const int j1 = p.n_query ? max(0, min(nq, p.n_query[b] - n0)) : nq;
+    // live queries: j0 <= j < j1 (positions >= 0, before the row's count, which may be any int32)
+    const int j1 = p.n_query ? (int)max((int64_t)0, min((int64_t)nq, (int64_t)p.n_query[b] - n0)) : nq;
     const int j0 = pos0 < 0 ? (int)min((int64_t)j1, -pos0) : 0;
     const int64_t row0 = (int64_t)b * p.Qn + n0;
     const int32_t *table = p.table + (int64_t)b * p.max_pages, *lists = p.blocks + row0 * p.n_slots;

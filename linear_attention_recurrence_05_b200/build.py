@@ -39,7 +39,11 @@ def _build_fast(force: bool) -> None:
     if not force and os.path.exists(FAST) and os.path.getmtime(FAST) >= newest:
         return
     import sysconfig
-    import torch
+    try:
+        import torch
+    except ImportError:
+        sys.stderr.write("no PyTorch: libgdn.so is built, the Python package's _fast.so is not\n")
+        return
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     tmp = f"{FAST}.{os.getpid()}.tmp"
@@ -50,7 +54,7 @@ def _build_fast(force: bool) -> None:
            "-ltorch_cpu", "-Wl,--no-as-needed", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {FAST_SRC}:\n{r.stderr}")
+        raise RuntimeError(f"libgdn.so is built, but g++ failed on {FAST_SRC}:\n{r.stderr}")
     os.replace(tmp, FAST)
 
 
@@ -63,12 +67,11 @@ def _compile(src: str) -> tuple:
     return obj, r.stderr
 
 
-def build(force: bool = False, jobs: int = 0, verbose: bool = False) -> str:
-    _build_fast(force)
+def _build_lib(force: bool, jobs: int, verbose: bool) -> None:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     newest = max(os.path.getmtime(p) for p in _deps() + [os.path.abspath(__file__)])
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
-        return LIB
+        return
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs))) as ex:
         results = list(ex.map(_compile, srcs))
@@ -81,6 +84,12 @@ def build(force: bool = False, jobs: int = 0, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def build(force: bool = False, jobs: int = 0, verbose: bool = False) -> str:
+    """Builds libgdn.so, which needs nvcc alone, then _fast.so where there is a PyTorch to build it for."""
+    _build_lib(force, jobs, verbose)
+    _build_fast(force)
     return LIB
 
 

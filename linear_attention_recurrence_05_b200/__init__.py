@@ -368,6 +368,9 @@ def _load_calls():
     global _calls
     try:
         from . import _fast
+        from .build import fast_key
+        if getattr(_fast, "built_for", None) != fast_key():
+            raise ImportError(f"it was built for {getattr(_fast, 'built_for', 'another PyTorch')}, this is {fast_key()}")
     except ImportError as e:
         raise RuntimeError("_fast.so is missing or does not fit this PyTorch: build it with "
                            "`python -m linear_attention_recurrence_05_b200.build`") from e

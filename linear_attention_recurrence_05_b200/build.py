@@ -23,6 +23,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 FAST_SRC = os.path.join(CSRC, "fast_calls.cpp")
 FAST = os.path.join(PKG, "_fast.so")
+FAST_KEY = os.path.join(BUILD, "_fast.key")          # what the present _fast.so was built for
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -34,28 +35,44 @@ def _deps() -> list:
                   glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def fast_key() -> str:
+    """The PyTorch and Python whose headers and object layouts are compiled into _fast.so."""
+    import torch
+    return (f"PyTorch {torch.__version__}, C++ ABI {int(torch.compiled_with_cxx11_abi())}, "
+            f"{sys.implementation.cache_tag} {sys.version.split()[0]}")
+
+
 def _build_fast(force: bool) -> None:
-    newest = max(os.path.getmtime(p) for p in [FAST_SRC, os.path.join(INCLUDE, "libgdn.h"), os.path.abspath(__file__)])
-    if not force and os.path.exists(FAST) and os.path.getmtime(FAST) >= newest:
-        return
-    import sysconfig
     try:
         import torch
     except ImportError:
         sys.stderr.write("no PyTorch: libgdn.so is built, the Python package's _fast.so is not\n")
         return
+    import sysconfig
+    key, built_for = fast_key(), None
+    if os.path.exists(FAST_KEY):
+        with open(FAST_KEY, encoding="utf-8") as f:
+            built_for = f.read()
+    newest = max(os.path.getmtime(p) for p in [FAST_SRC, os.path.join(INCLUDE, "libgdn.h"), os.path.abspath(__file__)])
+    if not force and os.path.exists(FAST) and os.path.getmtime(FAST) >= newest and built_for == key:
+        return
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     tmp = f"{FAST}.{os.getpid()}.tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f"-I{INCLUDE}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DGDN_BUILT_FOR="{key}"', f"-I{INCLUDE}",
            f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include", f"-I{cuda}/include",
            f"-I{sysconfig.get_path('include')}", FAST_SRC, "-o", tmp, f"-L{root}/lib", "-lc10", "-lc10_cuda", "-ltorch",
            "-ltorch_cpu", "-Wl,--no-as-needed", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"libgdn.so is built, but g++ failed on {FAST_SRC}:\n{r.stderr}")
+    os.makedirs(BUILD, exist_ok=True)
+    if os.path.exists(FAST_KEY):                          # (no moment at which the key describes another file)
+        os.remove(FAST_KEY)
     os.replace(tmp, FAST)
+    with open(FAST_KEY, "w", encoding="utf-8") as f:
+        f.write(key)
 
 
 def _compile(src: str) -> tuple:

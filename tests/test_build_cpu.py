@@ -1,4 +1,5 @@
-"""The build's host logic with stand-ins for the compilers: the C library needs nvcc alone."""
+"""The build's host logic with stand-ins for the compilers: the C library needs nvcc alone, and the Python
+package's host path is built for one PyTorch and Python."""
 import os
 import subprocess
 import sys
@@ -12,7 +13,7 @@ from linear_attention_recurrence_05_b200 import build as b
 def tree(repo_tmp, monkeypatch):
     """The build writing to a scratch directory; the compilers leave an empty output each.  Returns the
     commands that were run."""
-    for name, rel in (("LIB", "libgdn.so"), ("FAST", "_fast.so"), ("BUILD", "_build")):
+    for name, rel in (("LIB", "libgdn.so"), ("FAST", "_fast.so"), ("BUILD", "_build"), ("FAST_KEY", "_build/_fast.key")):
         monkeypatch.setattr(b, name, os.path.join(repo_tmp, rel))
     runs = []
 
@@ -50,3 +51,32 @@ def test_up_to_date_files_are_kept(tree):
     assert n > 2 and len(tree) == n
     b.build(force=True)
     assert len(tree) == 2 * n
+
+
+def test_host_path_is_built_again_for_another_pytorch(tree, monkeypatch):
+    import torch
+    b.build()
+    del tree[:]
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    b.build()
+    assert [cmd[0] for cmd in tree] == ["g++"] and any("PyTorch 0.0.0" in a for a in tree[0])
+    b.build()
+    assert len(tree) == 1
+    os.remove(b.FAST_KEY)                                # built for nobody knows what
+    b.build()
+    assert len(tree) == 2
+
+
+def test_host_path_says_what_it_was_built_for():
+    from linear_attention_recurrence_05_b200 import _fast
+    assert _fast.built_for == b.fast_key()
+
+
+def test_host_path_of_another_pytorch_is_not_called(monkeypatch):
+    import linear_attention_recurrence_05_b200 as gdn
+    from linear_attention_recurrence_05_b200 import _fast
+    monkeypatch.setattr(gdn, "_calls", None)
+    monkeypatch.setattr(_fast, "built_for", "PyTorch 0.0.0")
+    with pytest.raises(RuntimeError, match="_fast.so"):
+        gdn._load_calls()
+    assert gdn._calls is None

@@ -72,11 +72,24 @@ def test_host_path_says_what_it_was_built_for():
     assert _fast.built_for == b.fast_key()
 
 
-def test_host_path_of_another_pytorch_is_not_called(monkeypatch):
+@pytest.mark.parametrize("how", ["missing", "another"])
+def test_calls_without_a_fitting_host_path_go_through_python(how, monkeypatch):
+    """... with one warning, and with the Python way's own refusals."""
+    import torch
     import linear_attention_recurrence_05_b200 as gdn
     from linear_attention_recurrence_05_b200 import _fast
     monkeypatch.setattr(gdn, "_calls", None)
-    monkeypatch.setattr(_fast, "built_for", "PyTorch 0.0.0")
-    with pytest.raises(RuntimeError, match="_fast.so"):
-        gdn._load_calls()
-    assert gdn._calls is None
+    if how == "another":
+        monkeypatch.setattr(_fast, "built_for", "PyTorch 0.0.0")
+    else:
+        monkeypatch.delattr(gdn, "_fast")
+        monkeypatch.setitem(sys.modules, gdn.__name__ + "._fast", None)
+    q, w, pos = torch.zeros(1, 2, 4, 128, dtype=torch.bfloat16), torch.ones(128), torch.zeros(1, dtype=torch.int32)
+    with pytest.warns(RuntimeWarning, match="_fast.so"), pytest.raises(TypeError, match="CUDA"):
+        gdn.qsa_norm_rope(q, w, pos)
+    kc, tab, blocks = torch.zeros(2, 4, 8, 128, dtype=torch.bfloat16), torch.zeros(1, 2, dtype=torch.int32), pos.view(1, 1, 1)
+    with pytest.raises(TypeError, match="CUDA"):
+        gdn.qsa_kv_append(q, q, w, pos, tab, kc, kc)
+    with pytest.raises(TypeError, match="CUDA"):
+        gdn.qsa_attention(q[:, :1].contiguous(), blocks, pos, tab, kc, kc)
+    assert gdn._calls is gdn._NoCalls

@@ -11,8 +11,8 @@ states).  `e2e` repeats the prefill measurement through the public API from pinn
 host buffers, every step's copies included (uploads, kernels and downloads of
 consecutive steps overlap on three streams).  `roofline` describes the dominant prefill kernel,
 timed live with the library's launch trace; its `traffic` is the DRAM bytes of one launch from
-an ncu capture recorded in the profile summaries together with the sha256 of the kernel
-sources it was built from, and is null when the sources have changed since.  `step` gives the
+an ncu capture recorded in the profile summaries together with the sha256 of the kernel's own
+sources, and is null when those have changed since.  `step` gives the
 whole prefill step against the TF32 and bf16 tensor peaks.  `prefill_longctx` (T = 262,144,
 mean alpha 0.98) and `prefill_varlen` (32 packed sequences of log-uniform lengths with initial
 states) are the two other prefill workloads, each with its roofline and oracle baseline.
@@ -392,9 +392,8 @@ def code_only(text):
 
 def kernel_sources_sha256():
     """sha256 over the library's kernel and ABI sources (file names and code with comments
-    and blank lines removed, files sorted): the identity of the kernels whose DRAM traffic a
-    record describes.  An edit to a comment leaves it unchanged; any change to the code
-    changes it."""
+    and blank lines removed, files sorted): the identity of the library that ran.  An
+    edit to a comment leaves it unchanged; any change to the code changes it."""
     import hashlib
     h = hashlib.sha256()
     roots = [os.path.join(ROOT, "linear_attention_recurrence_05_b200", "csrc"), os.path.join(ROOT, "include")]
@@ -404,6 +403,35 @@ def kernel_sources_sha256():
                 h.update(name.encode())
                 with open(os.path.join(r, name), encoding="utf-8") as f:
                     h.update(code_only(f.read()).encode())
+    return h.hexdigest()
+
+
+_INCLUDE = re.compile(r'^[ \t]*#[ \t]*include[ \t]*"([^"]+)"', re.M)
+_PROTOTYPE = re.compile(r"^[A-Za-z_][\w \t*:&]*\([^;{}]*\)[ \t]*;", re.M)
+
+
+def own_sources_sha256(kernel):
+    """sha256 over what `kernel` is made of: `<kernel>.cu` and the headers that it includes, those
+    of its headers among them, less comments and blank lines, and less the `.h` files' function
+    prototypes (other files' functions).  The identity of the kernel whose DRAM traffic a record
+    describes: work on other kernels leaves it unchanged."""
+    import hashlib
+    roots = [os.path.join(ROOT, "linear_attention_recurrence_05_b200", "csrc"), os.path.join(ROOT, "include")]
+    code, todo = {}, [kernel + ".cu"]
+    while todo:
+        name = todo.pop()
+        path = next((p for p in (os.path.join(r, name) for r in roots) if os.path.exists(p)), None)
+        if name in code or path is None:
+            continue
+        with open(path, encoding="utf-8") as f:
+            code[name] = code_only(f.read())
+        todo += _INCLUDE.findall(code[name])
+        if name.endswith(".h"):
+            code[name] = code_only(_PROTOTYPE.sub("", code[name]))
+    h = hashlib.sha256()
+    for name in sorted(code):
+        h.update(name.encode())
+        h.update(code[name].encode())
     return h.hexdigest()
 
 
@@ -429,19 +457,20 @@ def traffic_records():
     return recs
 
 
-def traffic_for(kernel, workload, units_per_launch, sha):
+def traffic_for(kernel, workload, units_per_launch, sha=own_sources_sha256):
     """The recorded per-launch DRAM bytes of `kernel` scaled to `units_per_launch` (tokens or
     rows; the kernels' traffic grows in proportion to them), or None with the reason when no
-    record matches the sources that were built."""
+    record matches the sources that were built (`sha`: their hash, or the function that gives a
+    kernel's)."""
     r = traffic_records().get((kernel, workload))
     if r is None:
         return None, "no ncu record"
-    if r.get("sources_sha256") != sha:
+    if r.get("sources_sha256") != (sha(kernel) if callable(sha) else sha):
         return None, f"stale: {r['file']} was captured on other sources"
     return r["bytes_per_launch"] * units_per_launch / r["units_per_launch"], r["file"]
 
 
-def prefill_roofline(res, peaks, peak_src, sha):
+def prefill_roofline(res, peaks, peak_src, sha=own_sources_sha256):
     pk = res["per_kernel"]
     dom = max(pk, key=lambda n: pk[n]["total_ms"])
     avg_s = pk[dom]["avg_ms"] / 1e3
@@ -792,7 +821,7 @@ def bench_decode(args, dist, torch, gdn, peaks, peak_src):
     dist.barrier()
     e2e_ms = dist.max(e2.elapsed_time(e3))
     toks = B * steps * dist.world
-    dec_traffic, dec_tsrc = traffic_for("decode", w["name"], B, kernel_sources_sha256())
+    dec_traffic, dec_tsrc = traffic_for("decode", w["name"], B)
     multi = bench_decode_multi(args, dist, torch, gdn, peaks, peak_src, shape, cfg, (wq, wk, wv),
                                (dq, dk, dv, da, db), state, conv, state0, conv0)
     return {
@@ -965,9 +994,8 @@ def main():
             print(json.dumps({"metric": "QSA indexer query tokens/s", "qsa": qsa, "peaks": peak_src}), flush=True)
         dist.close()
         return
-    sha = kernel_sources_sha256()
     pre = bench_prefill(args, dist, torch, gdn, peaks)
-    roof = prefill_roofline(pre, peaks, peak_src, sha)
+    roof = prefill_roofline(pre, peaks, peak_src)
     more = {}
     if not args.no_long:
         for idx, key in ((2, "prefill_longctx"), (4, "prefill_varlen")):
@@ -976,7 +1004,7 @@ def main():
                          "ms_per_step": r["ms_per_step"], "steps": r["steps"], "n_seqs": r["n_seqs"],
                          "tokens_per_step": r["tokens_per_step"], "workspace_bytes": r["workspace_bytes"],
                          "gpu_launches_per_step": r["launches"], "clocks": r["clocks"],
-                         "roofline": prefill_roofline(r, peaks, peak_src, sha),
+                         "roofline": prefill_roofline(r, peaks, peak_src),
                          "step": prefill_step_summary(r, peaks), "kernels": r["per_kernel"]}
             torch.cuda.empty_cache()
     dec = None if args.no_decode else bench_decode(args, dist, torch, gdn, peaks, peak_src)
@@ -1007,7 +1035,8 @@ def main():
             "clocks": pre["clocks"], "e2e": pre["e2e"], "gpu_launches": pre["launches"] * args.steps,
             "roofline": roof, "step": prefill_step_summary(pre, peaks), "kernels": pre["per_kernel"],
             "cpu_baseline": cpu, "cpu_baseline_1core": cpu1, **more,
-            "decode": dec, "output_gate": tail, "prefill_gated": gated, "qsa": qsa, "peaks": peak_src, "sources_sha256": sha,
+            "decode": dec, "output_gate": tail, "prefill_gated": gated, "qsa": qsa, "peaks": peak_src,
+            "sources_sha256": kernel_sources_sha256(),
         }
         print(json.dumps(line), flush=True)
     dist.close()

@@ -165,3 +165,46 @@ def test_reference_arm_line(repo_tmp):
     r1 = subprocess.run(cmd, capture_output=True, text=True, cwd=repo_tmp,
                         env=dict(os.environ, RANK="1", WORLD_SIZE="2"), timeout=600)
     assert r1.returncode == 0 and not r1.stdout.strip()
+
+
+def test_a_kernels_hash_follows_its_own_sources(bench, repo_tmp, monkeypatch):
+    """Work on other kernels, prototypes of their functions and comments leave a kernel's hash as it is; its
+    file, the headers that it includes at any depth and the types in them do not."""
+    csrc = os.path.join("linear_attention_recurrence_05_b200", "csrc")
+    k, deep, h, other = (os.path.join(csrc, n) for n in ("k.cu", "deep.cuh", "k.h", "other.cu"))
+    api = os.path.join("include", "api.h")
+    files = {k: '#include "deep.cuh"\n#include <math.h>\n__global__ void k(float *p) { p[0] = kN; }\n',
+             deep: '#pragma once\n  #include "k.h"\n__device__ int f(int);\n',
+             h: '#include "api.h"\nstruct P {\n    int n;\n};\nconstexpr int kN = 64;\nint launch_k(const P &p,\n             int s);\n',
+             api: "typedef enum { A = 0 } e;\nEXPORT int api(int *a, int b);\n",
+             other: '#include "k.h"\n__global__ void other() {}\n'}
+    _tree(repo_tmp, files)
+    monkeypatch.setattr(bench, "ROOT", repo_tmp)
+    h0 = bench.own_sources_sha256("k")
+    same = [{other: "__global__ void other(int) {}\n"},
+            {h: files[h] + "// more\nint launch_other(const P &p, float x);\nvoid note(int);\n"},
+            {api: files[api] + "EXPORT int api2(int *a,\n                int b);\n"},
+            {os.path.join(csrc, "calls.cpp"): "int x;\n", os.path.join(csrc, "new.cuh"): "int y;\n"}]
+    changed = [{k: files[k].replace("p[0]", "p[1]")}, {deep: files[deep] + "__device__ int g();\n"},
+               {h: files[h].replace("64", "65")}, {h: files[h].replace("int n;", "long n;")},
+               {api: files[api].replace("A = 0", "A = 1")}]
+    for edit, keeps in [(e, True) for e in same] + [(e, False) for e in changed]:
+        _tree(repo_tmp, files)
+        assert bench.own_sources_sha256("k") == h0
+        _tree(repo_tmp, edit)
+        assert (bench.own_sources_sha256("k") == h0) is keeps, edit
+
+
+def test_traffic_lookup_takes_the_kernels_own_sources(bench, repo_tmp, monkeypatch):
+    csrc = os.path.join("linear_attention_recurrence_05_b200", "csrc")
+    _tree(repo_tmp, {os.path.join(csrc, "k.cu"): "int a;\n", os.path.join(csrc, "other.cu"): "int b;\n"})
+    monkeypatch.setattr(bench, "ROOT", repo_tmp)
+    rec = {"kernel": "k", "workload": "w", "bytes_per_launch": 100, "units_per_launch": 1, "unit": "rows",
+           "sources_sha256": bench.own_sources_sha256("k")}
+    _tree(repo_tmp, {os.path.join("profiles", "k.md"): "traffic-record: " + json.dumps(rec) + "\n"})
+    assert bench.traffic_for("k", "w", 2) == (200, "k.md")
+    _tree(repo_tmp, {os.path.join(csrc, "other.cu"): "int c;\n"})
+    assert bench.traffic_for("k", "w", 2) == (200, "k.md")
+    _tree(repo_tmp, {os.path.join(csrc, "k.cu"): "int c;\n"})
+    val, why = bench.traffic_for("k", "w", 2)
+    assert val is None and why.startswith("stale")

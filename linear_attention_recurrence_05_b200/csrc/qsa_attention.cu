@@ -469,7 +469,7 @@ static cudaError_t launch_single(AttnParams &p, cudaStream_t s) {
         cfg.attrs = &at;
         cfg.numAttrs = 1;
     }
-    TraceLaunch tl(s, "qsa_attention");
+    TraceLaunch tl(s, p.split > 1 ? "qsa_attention_split" : "qsa_attention");
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 

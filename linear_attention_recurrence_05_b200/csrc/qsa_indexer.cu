@@ -746,7 +746,9 @@ cudaError_t launch_qsa_topk(const float *scores, int64_t ld, const int32_t *qpos
     const size_t smem = (size_t)(qsa::kHist + 96) * 4 + (size_t)qsa::kCandCap * 8 +
                         (size_t)2 * ((nb_max + 31) / 32) * 4;
     auto kern = qsa::qsa_topk_kernel;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the same value (all that a CTA can have) at every call: host threads share the attribute, and this call's
+    // own size would lower it between another thread's setting and its launch
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
     if (e != cudaSuccess) return e;
     TraceLaunch tl(s, "qsa_topk");
     kern<<<(unsigned)((int64_t)B * Qn), qsa::kTopThr, smem, s>>>(p);

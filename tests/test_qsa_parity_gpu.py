@@ -343,3 +343,42 @@ def test_select_degenerate_rows():
     ov = [_check_row(bl[2, j], tk[2, j], s[j], A[j], int(pos[j]), qi.n_complete(pos[j], nblk[2]), sb[j])
           for j in range(Qn)]
     assert min(ov) >= 0.97
+
+
+def test_select_from_two_host_threads():
+    """Selections over long and over short caches from two host threads at once, each on a stream of its own,
+    all succeed and give the bits of a call alone."""
+    import threading
+    torch, gdn = _mods()
+    g = torch.Generator(device="cuda").manual_seed(77)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    w, jobs = torch.ones(128, device="cuda"), []
+    for nb in (20000, 600):
+        q, kbar = rnd(1, 1, 4, 128), rnd(1, nb, 128)
+        args = (q, w, _i32(torch, [4 * nb - 1]), kbar, _i32(torch, [nb]))
+        jobs.append((args, gdn.qsa_select(*args)[0]))
+    torch.cuda.synchronize()
+    select = gdn._native.lib().gdn_qsa_select
+    failed, wrong, gate = [0, 0], [0, 0], threading.Barrier(2)
+
+    def work(i):
+        args, want = jobs[i]
+        ws = torch.empty(gdn.qsa_select_workspace_size(1, 1, args[3].shape[1]) + 256, dtype=torch.uint8, device="cuda")
+        with torch.cuda.stream(torch.cuda.Stream()):
+            gate.wait()
+            q, w_q, qpos, kbar, n_blocks = args
+            got = torch.empty_like(want)
+            raw = (q.data_ptr(), w_q.data_ptr(), qpos.data_ptr(), kbar.data_ptr(), n_blocks.data_ptr(), 1, 1, kbar.shape[1],
+                   1e-6, 1e4, got.data_ptr(), None, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+            for n in range(60000):
+                failed[i] += select(*raw) != 0
+            wrong[i] += not torch.equal(got, want)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0, 0] and wrong == [0, 0]

@@ -375,10 +375,13 @@ cudaError_t launch_decode_multi(const DecodeParams &p, bool in_bf16, bool out_bf
     const int G = p.n_v / p.n_qk;
     // one state tile + gates + v of every (head, token)
     const int kPrefetch = kHeadDim * kHeadDim * 4 + 2 * G * p.n_tok * 4 + G * p.n_tok * kHeadDim * 4;
-    if (kPrefetch > 200 * 1024) return cudaErrorInvalidValue;
+    constexpr int kMost = 200 * 1024;
+    if (kPrefetch > kMost) return cudaErrorInvalidValue;
     auto k = in_bf16 ? (out_bf16 ? decode_multi_kernel<gdn::bf16, gdn::bf16> : decode_multi_kernel<gdn::bf16, float>)
                      : (out_bf16 ? decode_multi_kernel<float, gdn::bf16> : decode_multi_kernel<float, float>);
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrefetch);
+    // the same value at every call: host threads share the attribute, and this call's own size would lower it
+    // between another thread's setting and its launch
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
     TraceLaunch tl(s, "decode_multi");
     k<<<grid, kDecThreads, kPrefetch, s>>>(p);

@@ -234,3 +234,45 @@ def test_conv_silu_single_and_multi_token(lib, dtype):
     torch.cuda.synchronize()
     assert rel_err(np.swapaxes(to_host_f64(y), 0, 1), yo) <= tol(dtype)
     assert rel_err(to_host_f64(state), So) <= tol(dtype)
+
+
+def test_decode_multi_from_two_host_threads():
+    """Calls of 8 tokens and of 1 token from two host threads at once, each on a stream of its own, all
+    succeed and give the bits of a call alone."""
+    import ctypes
+    import threading
+    import torch
+    import linear_attention_recurrence_05_b200 as lib
+    g = torch.Generator(device="cuda").manual_seed(78)
+    H, Hv, jobs = 2, 6, []
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    w = [torch.randn((h * 128, 4), generator=g, device="cuda") * 0.3 for h in (H, H, Hv)]
+    for n in (8, 1):
+        q, k, v = rnd(1, n, H, 128), rnd(1, n, H, 128), rnd(1, n, Hv, 128)
+        a, b = (torch.rand((1, n, Hv), generator=g, device="cuda").bfloat16() for _ in range(2))
+        state = torch.randn((1, Hv, 128, 128), generator=g, device="cuda")
+        jobs.append(((q, k, v, *w, a, b), state, lib.gdn_decode_multi(q, k, v, *w, a, b, state.clone())))
+    torch.cuda.synchronize()
+    cfg, multi = lib.GdnConfig(H, Hv).c(), lib._native.lib().gdn_decode_multi
+    failed, wrong, gate = [0, 0], [0, 0], threading.Barrier(2)
+
+    def work(i):
+        x, state, want = jobs[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            s, got = state.clone(), torch.empty_like(want)
+            raw = (ctypes.byref(cfg), lib.GDN_BF16, lib.GDN_F32, *(t.data_ptr() for t in x), s.data_ptr(), None, None, 1, None, None,
+                   got.data_ptr(), 1, want.shape[1], torch.cuda.current_stream().cuda_stream)
+            gate.wait()
+            for n in range(60000):
+                failed[i] += multi(*raw) != 0
+            s.copy_(state)
+            failed[i] += multi(*raw) != 0
+            wrong[i] += not torch.equal(got, want)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0, 0] and wrong == [0, 0]

@@ -460,7 +460,8 @@ GDN_EXPORT gdn_status gdn_qsa_kv_append(const void *k, const void *v, gdn_dtype 
 /* Attention of the queries at positions i = qpos[b] + n, n < Qn, over
  *     S_i = tokens 4c .. 4c+3 of every listed block c, then the tail 4 floor((i+1)/4) .. i
  *     out[b][n][h] = softmax_{t in S_i}(scale <q[b][n][h], k_t>) V
- * in one pass (fp32 sums; the weights are rounded to bf16 for the second product).
+ * in one pass (fp32 sums).  The weights are rounded to bf16 for the second product: at most
+ * 2^-8 of sum w|v| beside the output's own rounding of 2^-8.
  *   q        bf16 [B][Qn][n_q_heads][d], normalised and rotated; out bf16, same shape
  *   blocks   int32 [B][Qn][n_slots]: gdn_qsa_select's block sets or any other list of blocks.
  *            Entries outside [0, floor((i+1)/4)) are skipped, in any place; an entry listed
@@ -469,8 +470,13 @@ GDN_EXPORT gdn_status gdn_qsa_kv_append(const void *k, const void *v, gdn_dtype 
  *            NULL: Qn
  * Blocks and tails on unmapped pages, or beyond max_pages pages, are skipped; unlisted and
  * skipped cache rows are never read, whatever they hold.  A query with no token (also one at a
- * negative position) gives zeros.  At most 16 query heads per key/value head.  The same inputs
- * give the same bits.  A bounded device-side wait that gives up (never expected) leaves NaN. */
+ * negative position) gives zeros, and so does a head whose every score is -infinity; a NaN score
+ * gives NaN.  At most 16 query heads per key/value head.  The same inputs give the same bits.
+ * Whether a call's queries are taken one by one or in tiles that share the union of their lists
+ * is decided by sizes alone, for lists of one row that agree about as much as scores of which
+ * half the variance is common to the row make them (q lists hold q^0.8 times the blocks of one):
+ * lists that agree more or less cost time, never the result.  A bounded device-side wait that
+ * gives up (never expected) leaves NaN. */
 GDN_EXPORT gdn_status gdn_qsa_attention(const void *q, const int32_t *blocks, int n_slots, const int32_t *qpos,
                                         const int32_t *n_query, int B, int Qn, const int32_t *page_table,
                                         int max_pages, int n_q_heads, int n_kv_heads, int head_dim,

@@ -4,7 +4,8 @@
 
 The library links the CUDA runtime statically, so it loads next to any PyTorch
 build; it exports only the C ABI of include/libgdn.h.  The Python package's native host path
-(csrc/fast_calls.cpp -> _fast.so) is compiled against the installed PyTorch.
+(csrc/fast_calls.cpp -> _fast.so) is compiled after it, against the installed PyTorch; where there is
+none the library alone is built, and the package's calls do without.
 """
 from __future__ import annotations
 

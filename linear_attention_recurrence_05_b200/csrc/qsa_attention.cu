@@ -21,7 +21,7 @@
 // 32 KB stages (128 tokens x 128 dims of K or V) pass through a ring, ordered K0 K1 V0 K2 V1 ..:
 // the scores of tile t + 1 are taken while the softmax of tile t runs.
 //
-// Bound by latency for a single token (128K tokens, 24 over 2 heads of 256: 9.8 us over 2 x 16 CTAs,
+// Bound by latency for a single token (128K tokens, 24 over 2 heads of 256: 9.9 us over 2 x 16 CTAs,
 // 12.5 over 2 x 8, of which the launch 2.5; the chain is list, page table, first keys, two products,
 // join), by HBM for some rows of a few tokens (16 x 4 at 32K: 39 us, 5 TB/s of distinct rows).  An MMA
 // of 16 columns takes 45 clk, not 8; transposed the other way round (heads on the 128 rows) one of 64
@@ -355,8 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_attention_kernel(const __grid
                 }
             }
             // P^T operand: row = column, column = token of this tile (bf16: the second product's
-            // operand type; relative error 2^-8 a term at most, independent between terms, so that
-            // the sum's stays below the output's own rounding).  A column without a score that compares
+            // operand type; a relative error of 2^-8 a term at most, independent between terms, so
+            // that a sum's is like the output's own rounding: 0.0018 of the outputs' rms in all for one
+            // token at 128K, 0.0017 of it that rounding alone).  A column without a score that compares
             // with its reference (all masked, or NaN) subtracts 0: masked tokens weigh 0, NaN ones NaN.
             unsigned char *pp = sp + (tok >> 6) * (NC * 128) + col0 * 128 + ((tok & 7) << 1);
             const int pc = (tok & 63) >> 3;
@@ -516,9 +517,9 @@ cudaError_t launch_qsa_attention(const void *q, const int32_t *blocks, int n_slo
     // waves of one CTA per SM times (a CTA's 64 KB of keys and values + its start and end), such
     // 64 KB taking a tile 1.27 (D 256) or 1.67 (D 128) times as long.  q queries' lists have about
     // q^0.8 times the tokens of one, at most those of the whole context.  Measured, single queries
-    // against tiles in us: 24 over 2 heads of 256 at 64K tokens, 16 queries 15 - 61, 64 30 - 62, 256
-    // 112 - 99, 1024 386 - 277; 16 over 4 heads of 128, 64 rows in 16 x 4 42 - 54, 256 queries 124 -
-    // 123, 1024 479 - 240; 4 x 200 queries at 4K 300 - 121.
+    // against tiles in us: 24 over 2 heads of 256 at 64K tokens, 16 queries 15 - 60, 64 30 - 62, 256
+    // 111 - 101, 1024 385 - 302; 16 over 4 heads of 128, 64 rows in 16 x 4 42 - 53, 256 queries 123 -
+    // 121, 1024 479 - 238; 4 x 200 queries at 4K 300 - 120.
     constexpr int kSms = 148;
     const double known = (double)max_pages * page, list = std::min(known, (double)n_slots * kR + 3.0);
     const double unit_tokens = 16384.0 / d;

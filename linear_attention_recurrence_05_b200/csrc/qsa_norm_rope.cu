@@ -27,7 +27,7 @@
 namespace gdn {
 namespace qsa_rows {
 
-// Small blocks start and leave evenly: 8192 tokens 41.7 us (43.7 with 8 warps, 41.4 with 2), fp32 3 x
+// Small blocks start and leave evenly: 8192 tokens 41.6 us (43.7 with 8 warps, 41.4 with 2), fp32 3 x
 // 1001 12.0 (12.7, 12.7), append of 8192 tokens 11.4 (11.7, 11.9).
 constexpr int kWarps = 4;
 constexpr int kMaxPairs = 128;   // rotated pairs of a head: at most 256 / 2

@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) qsa_attention_tile_kernel(const _
                     if (warp_live) {
                         // bf16, the second product's operand type: a relative error of 2^-8 a term at
                         // most, independent between terms, so that a sum's is like the output's own
-                        // rounding (0.0021 to 0.0023 of the outputs' rms in all, 0.0017 of it that
+                        // rounding (up to 0.0023 of the outputs' rms in all, 0.0017 of it that
                         // rounding alone); a second product for the rest of the weights would cost a
                         // tile 512 of its 1226 MMA clk again
                         const float m0 = m == -INFINITY ? 0.f : m;
